@@ -1099,6 +1099,7 @@ __global__ void __launch_bounds__(THREADS, 256 * kRowsPerSm / THREADS)
                 for (int m = 0; m < kMats; ++m) {
                     const uint32_t slot = use & 1u, bar = bars + slot * 8, phase = (use >> 1) & 1u;
                     cp_wait<1>();   // the next item's copies are one commit group
+                    __syncwarp();   // the scales are copies of all lanes, and each has waited for its own only
                     if (!dead && !mbar_try_wait(bar, phase))
                         dead = !mbar_wait(bar, phase, abort_flag, &g_w4_status, kWaitLimitNs);
                     if (__any_sync(0xffffffffu, dead)) {

@@ -526,7 +526,9 @@ int lmoe_balance_loss(const float *scores, int64_t T, int32_t E, int64_t ld, con
  * 32, 64 or 128.  Rows of codes start on 16 bytes: ld_codes is a multiple of
  * 16 and at least ceil(k / 2) rounded up to 16 (the bytes past the last column
  * may hold anything); ld_scales >= ceil(k / group).  A stack of matrices holds
- * one after the other, n * ld_codes bytes and n * ld_scales scales each.  The
+ * one after the other, n * ld_codes bytes and n * ld_scales scales each.  A
+ * scale that is infinite or NaN makes its group's weights NaN, whatever their
+ * codes, and with them every result that the group reaches.  The
  * pages describe no such format; it is an addition of this library. */
 typedef struct {
     const uint8_t *codes;

@@ -105,6 +105,20 @@ __device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&p)[4]) {
     }
 }
 
+// A row's sum, or NaN where it is infinite through one of the row's scales: the weights of such a
+// group are NaN.  (An infinite scale meets a group's sum that is 0 in one form and a rounding's residue
+// in another, so that the row's sum is NaN or an infinity, of which the softcaps would make a finite
+// number.)  The scales are looked at again for infinite sums only, so it costs nothing while the
+// weights stream past: within 1% in every case.
+__device__ __forceinline__ float settle(float v, const uint16_t *scales, int ng) {
+    if (fabsf(v) == __int_as_float(0x7f800000)) {
+#pragma unroll 1
+        for (int g = 0; g < ng; ++g)
+            if ((scales[g] & 0x7fffu) == 0x7f80u) v = __int_as_float(0x7fffffff);
+    }
+    return v;
+}
+
 // A matrix of 4-bit weights: n rows of k columns.
 struct Mat {
     const uint8_t *codes;
@@ -477,6 +491,7 @@ __global__ void __launch_bounds__(THREADS) __maxnreg__(P == 8 ? 128 : 96) w4_ker
         float *red = red0 + buf * red_size;
         const int u = c.u;
         const int tile0 = c.tile0;
+        const int expert = c.expert;
         do {
             int tile, kt;
             const bool there = task(c, tile, kt) >= 0;
@@ -574,7 +589,7 @@ __global__ void __launch_bounds__(THREADS) __maxnreg__(P == 8 ? 128 : 96) w4_ker
             const int tile = r >> 4, row = tile0 * 16 + r;
             if (MODE == MODE_MATVEC) {
                 if (row >= a.sh.n) continue;
-                const float v = sum(tile, r & 15, t);
+                const float v = settle(sum(tile, r & 15, t), a.m[0].scales + int64_t(row) * a.sh.lds, a.sh.ng);
                 const int64_t at = (entry * P + t) * a.ldy + row;
                 if (a.y_f32)
                     static_cast<float *>(a.y)[at] = v;
@@ -584,13 +599,22 @@ __global__ void __launch_bounds__(THREADS) __maxnreg__(P == 8 ? 128 : 96) w4_ker
                 if (row >= a.act_ld) continue;
                 float act = 0.f;   // features past the last one are zeros
                 if (row < a.sh.n) {
-                    const float p1 = sum(2 * tile, r & 15, t), p2 = sum(2 * tile + 1, r & 15, t);
+                    const int64_t sc = expert * a.mat_scales + int64_t(row) * a.sh.lds;
+                    const float p1 = settle(sum(2 * tile, r & 15, t), a.m[0].scales + sc, a.sh.ng);
+                    const float p2 = settle(sum(2 * tile + 1, r & 15, t), a.m[1].scales + sc, a.sh.ng);
                     act = situ_glu_exact(p1, p2, a.beta1, a.beta2);
                 }
                 a.act[entry * a.act_ld + row] = act;
             } else {
                 if (row >= a.sh.n) continue;
-                const float z = sum(tile, r & 15, 0);
+                float z = sum(tile, r & 15, 0);
+                if (fabsf(z) == __int_as_float(0x7f800000)) {
+#pragma unroll 1
+                    for (int j = 0; j < a.topk; ++j) {
+                        const int e = a.idx[entry * a.topk + j];
+                        if (e >= 0 && e < a.E) z = settle(z, a.m[0].scales + e * a.mat_scales + int64_t(row) * a.sh.lds, a.sh.ng);
+                    }
+                }
                 if (a.y_f32)
                     static_cast<float *>(a.y)[entry * a.ldy + row] = z;
                 else
@@ -1065,6 +1089,19 @@ __global__ void __launch_bounds__(THREADS, 256 * kRowsPerSm / THREADS)
         int left = n_steps, k = k_first;
         float acc[kMats][4];
         auto write = [&](int t) {
+            float most = 0.f;   // an infinity among the lane's sums (a NaN is passed over)
+#pragma unroll
+            for (int m = 0; m < kMats; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(acc[m][i]));
+            if (most == __int_as_float(0x7f800000)) {
+#pragma unroll
+                for (int m = 0; m < kMats; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[m][i] = settle(acc[m][i], a.m[m].scales + expert * a.mat_scales +
+                                                          int64_t(min(t * 16 + n + (i >> 1) * 8, a.sh.n - 1)) * a.sh.lds, a.sh.ng);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int row = t * 16 + n + (i >> 1) * 8, col = 2 * q + (i & 1);

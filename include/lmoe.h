@@ -546,7 +546,8 @@ int lmoe_w4_quantize(const uint16_t *w, int64_t rows, int32_t k, int64_t ld_w, i
 
 /* y[i] = W x[i] for the m rows of x: x [m][ld_x] bf16, y [m][ld_y] bf16 or, with
  * y_f32 = 1, fp32.  Sums in fp32, one rounding at the end.  For decode batches:
- * 0 <= m <= 64, 1 <= n, 1 <= k <= 65536; m = 0 enqueues nothing. */
+ * 0 <= m <= 64, 1 <= n, 1 <= k <= 65536; m = 0 enqueues nothing.  A row of x that holds
+ * an infinity or a NaN gives NaN throughout its row of y, and changes no other. */
 int lmoe_w4_matvec(const lmoe_w4 *w, int32_t n, int32_t k, int32_t group, const uint16_t *x, int32_t m, int64_t ld_x,
                    void *y, int64_t ld_y, int y_f32, cudaStream_t stream);
 
@@ -561,7 +562,8 @@ int lmoe_w4_experts_workspace_size(int32_t T, int32_t top_k, int32_t n_experts, 
  * w1, w2: stacks of n_experts matrices of inter rows and latent columns (one
  * ld_codes and one ld_scales for both); w3: of latent rows and inter columns.
  * h: [T][latent] bf16; topk_idx, gates: [T][top_k] (lmoe_forward's outputs); an
- * id outside [0, n_experts) adds nothing.  z: [T][latent] bf16; the activations enter
+ * id outside [0, n_experts) adds nothing.  A token whose h holds an infinity or a NaN has
+ * z NaN throughout.  z: [T][latent] bf16; the activations enter
  * W3 rounded to fp16's 11 bits, everything else is fp32 up to z.  0 <= T <= 1024, 1 <= top_k
  * <= 32, n_experts <= 1024, latent, inter <= 32768; T = 0 enqueues nothing.
  * workspace: 256-byte aligned, not shared with a call that may run at the same

@@ -263,12 +263,15 @@ __device__ __forceinline__ void run_task(uint32_t slot, const uint4 (&xf)[2 * P]
 }
 
 // Eight consecutive columns as fp16 pairs in fragment order, times up (the odd pairs times up / 16).
+// An infinity becomes NaN (h * 0 + h), so that its row gives NaN whether the codes are met as u - 8 or
+// with their offset, whose surplus comes off as infinity - infinity.
 __device__ __forceinline__ uint4 to_fragment(const float (&f)[8], float up) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float u = i & 1 ? up * 0.0625f : up;
-        const __half2 h = __floats2half2_rn(f[i] * u, f[i + 4] * u);
+        const __half2 v = __floats2half2_rn(f[i] * u, f[i + 4] * u);
+        const __half2 h = __hfma2(v, __floats2half2_rn(0.f, 0.f), v);
         w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);

@@ -125,3 +125,33 @@ def test_layer_with_weights_that_are_not_finite(lm, T, which):
     nan_only(y, (idx.cpu() == expert).any(1)[:, None].expand(T, shape.d))
     for one in (probe, h):
         lm.lmoe_destroy(one)
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("n", [64, 40000])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("k", [1000, 1001])
+@pytest.mark.parametrize("m", [1, 3, 8, 20])
+def test_matvec_with_activations_that_are_not_finite(lm, n, k, group, dtype, m):
+    """A row of x with an infinity gives NaN throughout its row of y, as one with a NaN does, in every form."""
+    codes, scales = lm.lmoe_w4_quantize(normal((n, k), 1).cuda(), group)
+    for at, value in ((0, INF), (k // 2, -INF), (k - 1, NAN)):
+        x = normal((m, k), at)
+        row = at % m
+        x[row, at] = value
+        where = torch.zeros(m, n, dtype=torch.bool)
+        where[row] = True
+        nan_only(lm.lmoe_w4_matvec(codes, scales, group, x.cuda(), out_dtype=dtype), where)
+
+
+@pytest.mark.parametrize("T", [1, 64])
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+def test_experts_with_activations_that_are_not_finite(lm, T, value):
+    q = [lm.lmoe_w4_quantize(t.cuda(), 32) for t in expert_weights()]
+    idx, gates = routing(T, E, K, T)
+    h = normal((T, L), 3)
+    t = T // 2
+    h[t, 111] = value
+    where = torch.zeros(T, L, dtype=torch.bool)
+    where[t] = True
+    nan_only(lm.lmoe_w4_experts(*q, 32, h.cuda(), idx.cuda(), gates.cuda()), where)

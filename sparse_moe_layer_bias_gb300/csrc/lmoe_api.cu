@@ -84,6 +84,16 @@ bool encoder_ready() {
     return g_encode != nullptr;
 }
 
+// Encodes a map.  The encoder wants a current context, which a host thread has only after a call of the
+// runtime that makes one (asking for the device does not): where it fails, once more with the thread's
+// device set.
+template <typename... Args>
+bool encode(Args... args) {
+    if (g_encode(args...) == CUDA_SUCCESS) return true;
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && g_encode(args...) == CUDA_SUCCESS;
+}
+
 // 2-D bf16 row-major [rows][cols] (row stride ld elements), box = 64 columns
 // (128 bytes, 128B swizzle) x box_rows rows.
 bool make_map(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint64_t ld,
@@ -92,11 +102,9 @@ bool make_map(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uin
     cuuint64_t strides[1] = {ld * 2};
     cuuint32_t box[2] = {64u, box_rows};
     cuuint32_t estr[2] = {1u, 1u};
-    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims,
-                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // 2-D fp32 row-major [rows][cols] (row stride ld elements) as a TMA store
@@ -106,10 +114,8 @@ bool make_store_map_f32(CUtensorMap *m, void *ptr, uint64_t rows, uint64_t cols,
     cuuint64_t strides[1] = {ld * 4};
     cuuint32_t box[2] = {32u, 32u};
     cuuint32_t estr[2] = {1u, 1u};
-    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, ptr, dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -406,9 +412,9 @@ bool make_w4_map(CUtensorMap *m, const lmoe_w4 *w, uint64_t rows, int64_t k) {
     cuuint64_t strides[1] = {cuuint64_t(w->ld_codes)};
     cuuint32_t box[2] = {128u, 16u};
     cuuint32_t estr[2] = {1u, 1u};
-    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(w->codes), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(w->codes), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 W4Weights w4_weights(const lmoe_w4 *w) { return W4Weights{w->codes, w->scales, w->ld_codes, w->ld_scales}; }

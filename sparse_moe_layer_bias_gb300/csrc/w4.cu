@@ -1367,6 +1367,8 @@ void make_shape(MatShape &sh, int n, int k, int group, int64_t ldc, int64_t lds,
     sh.full = sh.unit >= 8 ? std::min(sh.row_bytes / 256, sh.ng / (kTaskCols / group)) : 0;
 }
 
+// Of a block, and every kernel's limit: the limit belongs to the kernel, so a launch that set it to its own
+// size could lower it between another thread's setting and launch.
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kSmSmem = 228 * 1024;   // of an SM; a block takes 1 KB more than it asks for
 constexpr int kExpertRows = 4;   // rows of an entry where most experts have one: they leave room for two blocks on an SM
@@ -1397,7 +1399,7 @@ cudaError_t launch_w4(W4Args &a, int gpb, int cols, int64_t entries, int num_sms
     const int smem = plan<MODE, P>(a, cols, entries, num_sms);
     const int threads = a.cw * a.rw * 32;
     auto go = [&](auto kern) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
         if (e != cudaSuccess) return e;
         int per_sm = 1;
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, size_t(smem));
@@ -1456,7 +1458,7 @@ cudaError_t launch_rows(W4Args &a, const W4Maps &maps, int gpb, int rows, int64_
         grid = std::max<int64_t>(1, std::min<int64_t>(entries * tiles, int64_t(num_sms) * blocks));
     }
     auto go = [&](auto kern) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
         if (e != cudaSuccess) return e;
         return launch_kernel(kern, dim3(static_cast<unsigned>(grid)), dim3(warps * 32), size_t(smem), st, true, maps, ra);
     };

@@ -97,3 +97,42 @@ def test_a_backward_as_the_first_call_of_a_thread(lm):
                                                ptr(bws), bws.numel(), None)) == 0
     torch.cuda.synchronize()
     assert torch.equal(dx, want)
+
+
+def run_threads(calls, repeats):
+    """Each of `calls` `repeats` times in a thread and on a stream of its own; the statuses that are not 0."""
+    start, bad = threading.Barrier(len(calls)), []
+    streams = [torch.cuda.Stream() for _ in calls]
+
+    def loop(call, stream):
+        start.wait()
+        for _ in range(repeats):
+            st = call(ctypes.c_void_p(stream.cuda_stream))
+            if st:
+                bad.append(st)
+
+    threads = [threading.Thread(target=loop, args=a) for a in zip(calls, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return bad
+
+
+def check_together(made, repeats):
+    """Calls of different sizes at once: none disturbs another's launch (what a launch sets on a kernel, such as its
+    limit of shared memory, is seen by all threads; ctypes lets go of the interpreter during a call, so they do overlap)."""
+    torch.cuda.synchronize()
+    assert not run_threads([m[0] for m in made], repeats)
+    for _, y, want, _ in made:
+        assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("n", [64, 30000])
+def test_matvecs_of_different_widths_at_once(lm, n):
+    check_together([matvec(lm, n, k) for k in (64, 700, 2048, 5000)], 3000)
+
+
+def test_experts_of_different_widths_at_once(lm):
+    check_together([experts(lm, *a) for a in ((64, 64, 32), (64, 2048, 64), (64, 512, 1500), (1, 3584, 512), (2, 64, 40))], 1000)

@@ -521,10 +521,7 @@ cudaError_t launch_zero_unused(const int32_t *offsets, int E, int64_t per_expert
 cudaError_t launch_rms_bwd(const uint16_t *o, int64_t T, int k, int L, float eps, const uint16_t *dr, int64_t ld_dr,
                            uint16_t *dz, cudaStream_t stream) {
     if (T <= 0) return cudaSuccess;
-    const size_t smem = size_t(L) * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(rms_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+    const size_t smem = size_t(L) * sizeof(float);   // (latent <= 8192: within the 48 KB that every kernel may have)
     return launch_kernel(rms_bwd_kernel, dim3(static_cast<unsigned>(T)), dim3(kRmsThreads), smem, stream, true, o, k,
                          L, eps, dr, ld_dr, dz);
 }

@@ -70,7 +70,9 @@ __device__ __forceinline__ void store_rms_row(const float (&acc)[VPT][8], int L,
 }
 
 constexpr size_t kBulkRowsOffset = 64;          // the mbarrier and the abort flag come first
-constexpr size_t kBulkSmemMax = 227 * 1024;
+// Most of it, and the kernels' limit (one for all sizes: other host threads see it); the rest of a block's
+// 227 KB is for the sums.
+constexpr size_t kBulkSmemMax = 227 * 1024 - 128;
 
 // The same with the token's k rows in shared memory: warp 0's lanes issue one
 // bulk copy per row onto one mbarrier (armed first with all the bytes), every
@@ -241,7 +243,7 @@ cudaError_t launch_combine_rmsnorm(const uint16_t *o, int64_t T, int k, int L, f
     const size_t smem = kBulkRowsOffset + size_t(k) * size_t(L) * 2;
     if (L % 8 == 0 && (reinterpret_cast<uintptr_t>(o) % 16) == 0 && smem <= kBulkSmemMax) {
         auto bulk = [&](auto kern) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBulkSmemMax);
             if (e != cudaSuccess) return e;
             return launch_kernel(kern, grid, block, smem, st, true, o, k, L, eps, r, err, wait_limit_ns);
         };

@@ -289,10 +289,11 @@ cudaError_t launch_qb_histogram(const float *scores, int64_t T, int E, int64_t l
     const int64_t rows_per_chunk = (T + n_chunks - 1) / n_chunks;
     const unsigned grid = static_cast<unsigned>(n_groups) * static_cast<unsigned>(n_chunks);
 
+    // (the limit is one for all sizes: other host threads see it)
 #define LMOE_QB_VEC(N_, P_, U_)                                                                     \
     case N_:                                                                                        \
         err = cudaFuncSetAttribute(qb_hist_vec_kernel<N_, P_, U_>,                                  \
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);         \
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kHistSmemBudget); \
         if (err != cudaSuccess) return err;                                                         \
         qb_hist_vec_kernel<N_, P_, U_><<<grid, kHistThreads, smem, st>>>(scores, T, E, ld, B, hist,  \
                                                                          n_groups, rows_per_chunk); \
@@ -314,7 +315,7 @@ cudaError_t launch_qb_histogram(const float *scores, int64_t T, int E, int64_t l
         }
     } else {
         err = cudaFuncSetAttribute(qb_hist_scalar_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   (int)smem);
+                                   (int)kHistSmemBudget);
         if (err != cudaSuccess) return err;
         qb_hist_scalar_kernel<<<grid, kHistThreads, smem, st>>>(scores, T, E, ld, B, hist, epc,
                                                                n_groups, rows_per_chunk);

@@ -1,5 +1,6 @@
 """Calls from host threads other than the one that set up the GPU."""
 import ctypes
+import dataclasses
 import threading
 
 import pytest
@@ -136,3 +137,42 @@ def test_matvecs_of_different_widths_at_once(lm, n):
 
 def test_experts_of_different_widths_at_once(lm):
     check_together([experts(lm, *a) for a in ((64, 64, 32), (64, 2048, 64), (64, 512, 1500), (1, 3584, 512), (2, 64, 40))], 1000)
+
+
+def test_layers_of_different_widths_at_once(lm):
+    """top_k and latent set the sizes of the sum over a token's experts."""
+    tiny = synth.TINY
+    made = [layer(lm, 8, dataclasses.replace(tiny, latent=latent, top_k=k)) for latent, k in ((128, 1), (512, 4), (1024, 16), (2048, 30))]
+    made += [layer(lm, 8, dataclasses.replace(tiny, latent=latent), expert_w4=32) for latent in (256, 1536)]
+    check_together(made, 300)
+
+
+def backward(lm, shape, T):
+    lib = lm.load_library()
+    w = {k: v.cuda() for k, v in synth.layer_weights_host(shape).items()}
+    x, b = (t.cuda() for t in synth.activations_host(shape, T=T))
+    dy = synth.grad_output_host(shape, T=T).cuda()
+    h = lm.lmoe_create(dict(shape.layer_dict(), with_backward=True), w, max_tokens=T)
+    ws, dx = lm.alloc_workspace(h, T), torch.empty_like(x)
+    lm.lmoe_forward(h, x, b, workspace=ws)
+    want = lm.lmoe_backward(h, x, dy, ws)[0]
+    grads = {n: torch.empty(s, device="cuda") for n, s in lm.grad_shapes(h).items()}
+    g = binding.LmoeGrads(*[grads[n].data_ptr() for n in binding.WEIGHT_NAMES], 0)
+    bws = torch.empty(lm.lmoe_backward_workspace_size(h, T), dtype=torch.uint8, device="cuda")
+    call = lambda s: lib.lmoe_backward(h.ptr, ptr(x), T, ptr(dy), None, None, ptr(ws), ws.numel(), ptr(dx), ctypes.byref(g),
+                                       ptr(bws), bws.numel(), s)
+    return call, dx, want, (h, w, x, b, dy, ws, grads, bws)
+
+
+def test_backwards_of_different_widths_at_once(lm):
+    check_together([backward(lm, dataclasses.replace(synth.TINY, latent=latent), 8) for latent in (128, 512, 2048)], 100)
+
+
+def test_histograms_of_different_bins_at_once(lm):
+    lib, made = lm.load_library(), []
+    for E, B in ((64, 100), (64, 1000), (64, 3000), (61, 50), (61, 4000)):
+        s = torch.rand(300, E, device="cuda")
+        hist = torch.empty((E, B), dtype=torch.int32, device="cuda")
+        made.append((lambda st, s=s, E=E, B=B, hist=hist: lib.qb_histogram(ptr(s), 300, E, E, B, ptr(hist), 0, st), hist,
+                     lm.qb_histogram(s, B), s))
+    check_together(made, 2000)

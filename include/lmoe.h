@@ -417,7 +417,8 @@ int lmoe_selftest_timeout(lmoe_handle *handle, uint64_t limit_ns, cudaStream_t s
  * in a debug build also failed index checks).  Synchronises `stream`, copies
  * the status word, and clears it when `clear` is non-zero.  *device_status is
  * LMOE_OK, LMOE_ERR_TIMEOUT or (debug builds) LMOE_ERR_INDEX, which takes
- * precedence.  The index-check words are per library, not per handle. */
+ * precedence.  The index-check words are per library, not per handle (reading
+ * them, a debug build also waits for the streams that the legacy one waits for). */
 int lmoe_device_status(lmoe_handle *handle, cudaStream_t stream, int clear, int *device_status);
 
 /* 1 if this library was built with index checks (-DLMOE_DEBUG), else 0.
@@ -550,6 +551,18 @@ int lmoe_w4_quantize(const uint16_t *w, int64_t rows, int32_t k, int64_t ld_w, i
  * an infinity or a NaN gives NaN throughout its row of y, and changes no other. */
 int lmoe_w4_matvec(const lmoe_w4 *w, int32_t n, int32_t k, int32_t group, const uint16_t *x, int32_t m, int64_t ld_x,
                    void *y, int64_t ld_y, int y_f32, cudaStream_t stream);
+
+/* Device-side status of the calls here that take no handle (lmoe_w4_matvec,
+ * lmoe_w4_experts), as lmoe_device_status gives it for a handle's kernels (the
+ * 4-bit experts of lmoe_forward among them): LMOE_ERR_TIMEOUT after a bounded wait
+ * of theirs gave up, whose results are then not all written.  One word for the
+ * current device, so it does not say which call it was, and one report may stand
+ * for several.  Synchronises `stream`, which no other stream has to wait for. */
+int lmoe_w4_status(cudaStream_t stream, int clear, int *device_status);
+
+/* lmoe_selftest_timeout for that status: no handle, and lmoe_w4_status then
+ * reports LMOE_ERR_TIMEOUT. */
+int lmoe_w4_selftest_timeout(uint64_t limit_ns, cudaStream_t stream);
 
 /* Bytes of device workspace lmoe_w4_experts needs; never decreases with T. */
 int lmoe_w4_experts_workspace_size(int32_t T, int32_t top_k, int32_t n_experts, int32_t latent, int32_t inter,

@@ -38,6 +38,8 @@ from .binding import (  # noqa: F401
     lmoe_w4_experts_workspace_size,
     lmoe_w4_matvec,
     lmoe_w4_quantize,
+    lmoe_w4_selftest_timeout,
+    lmoe_w4_status,
     lmoe_workspace_layout,
     lmoe_workspace_size,
     load_library,

@@ -28,7 +28,8 @@ EXPORTED = ("lmoe_status_string", "lmoe_create", "lmoe_destroy", "lmoe_workspace
             "lmoe_route_static", "lmoe_debug_checks", "lmoe_selftest_index",
             "lmoe_selftest_timeout", "lmoe_backward_workspace_size", "lmoe_backward", "lmoe_backward_scores",
             "qb_histogram", "qb_quantile_bias", "qb_sign_update", "lmoe_balance_loss_workspace_size", "lmoe_balance_loss",
-            "lmoe_w4_quantize", "lmoe_w4_matvec", "lmoe_w4_experts_workspace_size", "lmoe_w4_experts")
+            "lmoe_w4_quantize", "lmoe_w4_matvec", "lmoe_w4_experts_workspace_size", "lmoe_w4_experts",
+            "lmoe_w4_status", "lmoe_w4_selftest_timeout")
 
 STAGES = ("down", "shared", "router", "topk", "scan", "offsets", "scatter", "expert_w12_light",
           "expert_w12_heavy", "expert_w3", "combine", "up")
@@ -147,6 +148,8 @@ def load_library():
         "lmoe_w4_quantize": [P, I64, I32, I64, I32, P, I64, P, I64, P],
         "lmoe_w4_matvec": [W4, I32, I32, I32, P, I32, I64, P, I64, ctypes.c_int, P],
         "lmoe_w4_experts_workspace_size": [I32, I32, I32, I32, I32, ctypes.POINTER(SZ)],
+        "lmoe_w4_status": [P, ctypes.c_int, ctypes.POINTER(ctypes.c_int)],
+        "lmoe_w4_selftest_timeout": [ctypes.c_uint64, P],
         "lmoe_w4_experts": [W4, W4, W4, I32, I32, I32, I32, P, I32, P, P, I32, F32, F32, P, P, SZ, P],
     }.items():
         getattr(lib, name).restype = ctypes.c_int
@@ -584,6 +587,19 @@ def lmoe_w4_matvec(codes: torch.Tensor, scales: torch.Tensor, group: int, x: tor
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError("out_dtype must be bfloat16 or float32")
     return (_calls or _native_calls()).w4_matvec(codes, scales, group, x, y, out_dtype is torch.float32, stream)
+
+
+def lmoe_w4_status(clear: bool = True, stream=None) -> int:
+    """Status of the 4-bit calls that take no handle, on the current device: 6 (LMOE_ERR_TIMEOUT) after a wait of
+    theirs gave up, else 0.  Synchronises the stream."""
+    v = ctypes.c_int()
+    _check("lmoe_w4_status", load_library().lmoe_w4_status(_stream(stream), 1 if clear else 0, ctypes.byref(v)))
+    return v.value
+
+
+def lmoe_w4_selftest_timeout(limit_ns: int = 1_000_000, stream=None):
+    """Enqueue the bounded-wait self-test for lmoe_w4_status (see include/lmoe.h)."""
+    _check("lmoe_w4_selftest_timeout", load_library().lmoe_w4_selftest_timeout(int(limit_ns), _stream(stream)))
 
 
 def lmoe_w4_experts_workspace_size(T: int, top_k: int, n_experts: int, latent: int, inter: int) -> int:

@@ -365,8 +365,8 @@ bool w4_wants_maps(int n, int k, int m, bool vec, int num_sms);
 // maps: of the matrix (both the same), or nullptr where w4_wants_maps is false.
 cudaError_t launch_w4_matvec(const W4Weights &w, int n, int k, int group, const uint16_t *x, int m, int64_t ldx, void *y,
                              int64_t ldy, int y_f32, const W4Maps *maps, int num_sms, cudaStream_t stream);
-// kDevErrTimeout when a wait of the 4-bit kernels gave up (one word for the library).
-unsigned w4_status_word(bool clear);
+// The word of the current device in which waits of calls without a handle leave kDevErrTimeout.
+cudaError_t w4_status_word(unsigned **word);
 // Scratch for so many x rows of k columns as the grouped path prepares them.
 size_t w4_x_bytes(int64_t rows, int k);
 // Row stride of the activations: inter up to a multiple of 128.
@@ -392,6 +392,7 @@ struct W4Experts {
     int norm;
     float rms_eps;
     float *zf;               // with norm, token by token: scratch [T][L]
+    unsigned *err;           // status word for waits that give up; nullptr: w4_status_word's
 };
 // W4Experts::most for x's T, topk, E, L, I and group.
 int w4_entry_rows(const W4Experts &x);

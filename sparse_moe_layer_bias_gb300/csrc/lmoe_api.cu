@@ -331,6 +331,15 @@ GemmArgs base_args(const lmoe_handle *h) {
     return a;
 }
 
+// The value of a status word once `stream` has come so far; cleared with `clear`.
+bool read_status(unsigned *word, cudaStream_t stream, bool clear, unsigned *v) {
+    if (cudaMemcpyAsync(v, word, sizeof *v, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess)
+        return false;
+    return !clear || !*v ||
+           (cudaMemsetAsync(word, 0, sizeof *v, stream) == cudaSuccess && cudaStreamSynchronize(stream) == cudaSuccess);
+}
+
 int gemm_status(cudaError_t e) { return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA; }
 
 // A dense GEMM of a small batch as split-K: the GEMM's fp32 epilogue writes
@@ -972,6 +981,7 @@ int lmoe_forward(lmoe_handle *h, const uint16_t *x, int64_t T, const float *bias
         a.ldz = L;
         a.norm = 1;
         a.rms_eps = c.rms_eps;
+        a.err = h->d_status;
         if (w4_scratch(a, ws + l.w4, w4_layout(T, K, E, L, I))) {
             a.maps12 = h->w4_maps12;
             a.maps3 = h->w4_maps3;
@@ -1609,21 +1619,12 @@ int lmoe_selftest_timeout(lmoe_handle *h, uint64_t limit_ns, cudaStream_t stream
 int lmoe_device_status(lmoe_handle *h, cudaStream_t stream, int clear, int *device_status) {
     if (!h || !device_status) return LMOE_ERR_INVALID_ARG;
     unsigned v = 0;
-    if (cudaMemcpyAsync(&v, h->d_status, sizeof v, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess)
-        return LMOE_ERR_CUDA;
-    if (clear && v) {
-        if (cudaMemsetAsync(h->d_status, 0, sizeof v, stream) != cudaSuccess ||
-            cudaStreamSynchronize(stream) != cudaSuccess)
-            return LMOE_ERR_CUDA;
-    }
+    if (!read_status(h->d_status, stream, clear != 0, &v)) return LMOE_ERR_CUDA;
     // a debug build's failed index checks (every translation unit's word)
     const bool cl = clear != 0;
     const unsigned dbg = debug_word_gemm(cl) | debug_word_pair(cl) | debug_word_split(cl) | debug_word_gemm_bwd(cl) | debug_word_route(cl) |
                          debug_word_backward(cl) | debug_word_selftest(cl);
-    const unsigned w4 = w4_status_word(cl);   // the 4-bit kernels' waits (one word per library)
-    if (dbg == ~0u || w4 == ~0u) return LMOE_ERR_CUDA;
-    v |= w4;
+    if (dbg == ~0u) return LMOE_ERR_CUDA;
     *device_status = dbg ? LMOE_ERR_INDEX : (v & kDevErrTimeout) ? LMOE_ERR_TIMEOUT : LMOE_OK;
     return LMOE_OK;
 }
@@ -1803,6 +1804,22 @@ int lmoe_w4_matvec(const lmoe_w4 *w, int32_t n, int32_t k, int32_t group, const 
     }
     return launch_w4_matvec(w4_weights(w), n, k, group, x, m, ld_x, y, ld_y, y_f32, tma ? &maps : nullptr, sms, stream) ==
                    cudaSuccess
+               ? LMOE_OK
+               : LMOE_ERR_CUDA;
+}
+
+int lmoe_w4_status(cudaStream_t stream, int clear, int *device_status) {
+    if (!device_status) return LMOE_ERR_INVALID_ARG;
+    unsigned *word = nullptr, v = 0;
+    if (w4_status_word(&word) != cudaSuccess || !read_status(word, stream, clear != 0, &v)) return LMOE_ERR_CUDA;
+    *device_status = (v & kDevErrTimeout) ? LMOE_ERR_TIMEOUT : LMOE_OK;
+    return LMOE_OK;
+}
+
+int lmoe_w4_selftest_timeout(uint64_t limit_ns, cudaStream_t stream) {
+    if (limit_ns < 1000ull || limit_ns > 1000000000ull) return LMOE_ERR_INVALID_ARG;
+    unsigned *word = nullptr;
+    return w4_status_word(&word) == cudaSuccess && launch_bounded_wait_selftest(word, limit_ns, nullptr, stream) == cudaSuccess
                ? LMOE_OK
                : LMOE_ERR_CUDA;
 }

@@ -388,6 +388,7 @@ struct W4Args {
     int64_t ldy;
     int y_f32;
     float *o;               // W3 grouped: [T * k][n] fp32
+    unsigned *err;          // status word of the caller's handle, or nullptr: the library's
 };
 
 // A unit is rt row tiles of one matrix (W12: of W1 and of W2; W3 by token: of each of the
@@ -660,7 +661,7 @@ constexpr int scale_row(bool aligned) { return kItemBoxes * 16 + (aligned ? 0 : 
 constexpr int item_scales(bool aligned) { return 16 * scale_row(aligned); }
 constexpr int kRowsPerSm = 2;             // blocks of 8 warps
 constexpr uint64_t kWaitLimitNs = 2000000000ull;        // 2 s per wait for a copy
-__device__ unsigned g_w4_status;                        // kDevErrTimeout when a wait gave up
+__device__ unsigned g_w4_status;                        // kDevErrTimeout when a wait of a call without a handle gave up
 
 // (u0, u4), (u1, u5), (u2, u6), (u3, u7) as 1024 + u or, the odd pairs, 16 (64 + u)
 __device__ __forceinline__ void unpack8_raw(uint32_t w, uint32_t (&v)[4]) {
@@ -902,6 +903,7 @@ __global__ void __launch_bounds__(THREADS, 256 * kRowsPerSm / THREADS)
     float4 *heads = reinterpret_cast<float4 *>(smem + at + 160 + warps * 16 + 16);   // [warp][matrix]: sums of a tile that another warp began
     const uint32_t bars = base + at + 160 + warp * 16;
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + at + 160 + warps * 16);
+    auto err = [&] { return a.err ? a.err : &g_w4_status; };
     if (lane < 2) mbar_init(bars + lane * 8, 1);
     if (threadIdx.x == 0) *abort_flag = 0u;
     fence_mbar_init();
@@ -1141,7 +1143,7 @@ __global__ void __launch_bounds__(THREADS, 256 * kRowsPerSm / THREADS)
                     cp_wait<1>();   // the next item's copies are one commit group
                     __syncwarp();   // the scales are copies of all lanes, and each has waited for its own only
                     if (!dead && !mbar_try_wait(bar, phase))
-                        dead = !mbar_wait(bar, phase, abort_flag, &g_w4_status, kWaitLimitNs);
+                        dead = !mbar_wait(bar, phase, abort_flag, err(), kWaitLimitNs);
                     if (__any_sync(0xffffffffu, dead)) {
                         dead = true;
                     } else {
@@ -1202,7 +1204,7 @@ __global__ void __launch_bounds__(THREADS, 256 * kRowsPerSm / THREADS)
     cp_wait<0>();
     // after a wait that gave up: leave no copy in flight
     for (; use < get; ++use)
-        mbar_wait(bars + (use & 1u) * 8, (use >> 1) & 1u, abort_flag, &g_w4_status, kWaitLimitNs, false);
+        mbar_wait(bars + (use & 1u) * 8, (use >> 1) & 1u, abort_flag, err(), kWaitLimitNs, false);
 }
 
 // Assignments grouped by expert: perm, and a list {expert, first place, rows} of the
@@ -1494,15 +1496,7 @@ cudaError_t launch_w4_quantize(const uint16_t *w, int64_t rows, int k, int64_t l
     return go(w4_quantize_kernel<128>);
 }
 
-unsigned w4_status_word(bool clear) {
-    unsigned v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_w4_status, sizeof v) != cudaSuccess) return ~0u;
-    if (clear && v) {
-        const unsigned z = 0;
-        if (cudaMemcpyToSymbol(g_w4_status, &z, sizeof z) != cudaSuccess) return ~0u;
-    }
-    return v;
-}
+cudaError_t w4_status_word(unsigned **word) { return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_w4_status); }
 
 // w4_rows_kernel starts later (the x rows first, which takes longer the more columns there are), then
 // streams faster and unpacks a weight once for 8 rows.  Measured (w4_kernel | w4_rows_kernel, us):
@@ -1595,6 +1589,7 @@ cudaError_t launch_w4_experts(const W4Experts &x, int num_sms, cudaStream_t st) 
     b.act_ld = w4_act_ld(x.I);
     b.beta1 = x.beta1;
     b.beta2 = x.beta2;
+    b.err = x.err;
     const int64_t entries = x.list ? std::min(n, std::min(n, x.E) + n / x.most) : n;
     {   // a = SiTU(W1 h) softcap(W2 h)
         W4Args a = b;

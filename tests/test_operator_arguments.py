@@ -135,3 +135,9 @@ def test_w4_handle_refuses(lib, change, status):
         setattr(cfg, k, v)
     w, out = binding.LmoeWeights(), ctypes.c_void_p()
     assert lib.lmoe_create(ctypes.byref(cfg), ctypes.byref(w), ctypes.byref(out)) == status
+
+
+def test_w4_status_refuses(lib):
+    assert lib.lmoe_w4_status(None, 0, None) == INVALID
+    assert lib.lmoe_w4_selftest_timeout(999, None) == INVALID
+    assert lib.lmoe_w4_selftest_timeout(1_000_000_001, None) == INVALID

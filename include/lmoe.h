@@ -547,7 +547,7 @@ int lmoe_w4_quantize(const uint16_t *w, int64_t rows, int32_t k, int64_t ld_w, i
 
 /* y[i] = W x[i] for the m rows of x: x [m][ld_x] bf16, y [m][ld_y] bf16 or, with
  * y_f32 = 1, fp32.  Sums in fp32, one rounding at the end.  For decode batches:
- * 0 <= m <= 64, 1 <= n, 1 <= k <= 65536; m = 0 enqueues nothing.  A row of x that holds
+ * 0 <= m <= 64, 1 <= n <= 2^31 - 4096, 1 <= k <= 65536; m = 0 enqueues nothing.  A row of x that holds
  * an infinity or a NaN gives NaN throughout its row of y, and changes no other. */
 int lmoe_w4_matvec(const lmoe_w4 *w, int32_t n, int32_t k, int32_t group, const uint16_t *x, int32_t m, int64_t ld_x,
                    void *y, int64_t ld_y, int y_f32, cudaStream_t stream);

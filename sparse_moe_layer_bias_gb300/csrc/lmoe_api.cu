@@ -1703,6 +1703,7 @@ int check_w4(const lmoe_w4 *w, int32_t k, int32_t group) {
 
 
 constexpr int32_t kW4MaxCols = 65536;
+constexpr int32_t kW4MaxRows = INT32_MAX - 4095;   // (a unit's row tiles may pass the last row by 64, in 32 bits)
 constexpr int32_t kW4MaxWidth = 32768;
 
 int check_w4_experts(int32_t T, int32_t top_k, int32_t E, int32_t L, int32_t I) {
@@ -1788,7 +1789,7 @@ int lmoe_w4_matvec(const lmoe_w4 *w, int32_t n, int32_t k, int32_t group, const 
                    void *y, int64_t ld_y, int y_f32, cudaStream_t stream) {
     if (n < 1 || k < 1 || m < 0 || !w4_group_ok(group) || ld_x < k || ld_y < n || (y_f32 != 0 && y_f32 != 1))
         return LMOE_ERR_INVALID_ARG;
-    if (m > 64 || k > kW4MaxCols) return LMOE_ERR_UNSUPPORTED_SHAPE;
+    if (m > 64 || k > kW4MaxCols || n > kW4MaxRows) return LMOE_ERR_UNSUPPORTED_SHAPE;
     int st = check_w4(w, k, group);
     if (st) return st;
     if (m == 0) return LMOE_OK;

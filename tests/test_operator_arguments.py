@@ -141,3 +141,8 @@ def test_w4_status_refuses(lib):
     assert lib.lmoe_w4_status(None, 0, None) == INVALID
     assert lib.lmoe_w4_selftest_timeout(999, None) == INVALID
     assert lib.lmoe_w4_selftest_timeout(1_000_000_001, None) == INVALID
+
+
+@pytest.mark.parametrize("n", [(1 << 31) - 1, (1 << 31) - 4095])
+def test_w4_matvec_refuses_more_rows_than_it_counts(lib, n):
+    assert matvec(lib, n=n, ldy=n) == SHAPE

@@ -103,7 +103,9 @@ typedef struct {
                            * many columns of a weight row (lmoe_w4_quantize's
                            * values; about 0.56 bytes a weight with 32).  Each
                            * forward runs them as lmoe_w4_experts does, and the
-                           * RMSNorm on its fp32 sum z.  For max_tokens <= 1024,
+                           * RMSNorm on its fp32 sum z.  Made for batches up to some
+                           * hundred tokens (at 1024, expert_fp8 is faster at K3's
+                           * widths).  For max_tokens <= 1024,
                            * not together with expert_fp8 or with_backward (else
                            * LMOE_ERR_UNSUPPORTED_SHAPE).  An addition of this
                            * library. */
@@ -546,7 +548,15 @@ int lmoe_w4_quantize(const uint16_t *w, int64_t rows, int32_t k, int64_t ld_w, i
                      int64_t ld_codes, uint16_t *scales, int64_t ld_scales, cudaStream_t stream);
 
 /* y[i] = W x[i] for the m rows of x: x [m][ld_x] bf16, y [m][ld_y] bf16 or, with
- * y_f32 = 1, fp32.  Sums in fp32, one rounding at the end.  For decode batches:
+ * y_f32 = 1, fp32.  Sums in fp32, one rounding at the end:
+ *   - x is held relative to the largest finite value of its row (or of 512 columns of it), to
+ *     2^-35 of that: smaller values may count as 0, also where the large one meets a
+ *     weight of 0.
+ *   - bf16 results of larger products are summed with the codes as they are (1024 + u, or
+ *     16 (64 + u)) from a start that takes the surplus off.  The partial sums are up to 225
+ *     times the result's usual size, which costs some 2^-16 of it, at most
+ *     24 * 2^-23 * 1152 sum |x s|.  fp32 results sum u - 8 itself.
+ * For decode batches:
  * 0 <= m <= 64, 1 <= n <= 2^31 - 4096, 1 <= k <= 65536; m = 0 enqueues nothing.  A row of x that holds
  * an infinity or a NaN gives NaN throughout its row of y, and changes no other. */
 int lmoe_w4_matvec(const lmoe_w4 *w, int32_t n, int32_t k, int32_t group, const uint16_t *x, int32_t m, int64_t ld_x,
@@ -577,7 +587,9 @@ int lmoe_w4_experts_workspace_size(int32_t T, int32_t top_k, int32_t n_experts, 
  * h: [T][latent] bf16; topk_idx, gates: [T][top_k] (lmoe_forward's outputs); an
  * id outside [0, n_experts) adds nothing.  A token whose h holds an infinity or a NaN has
  * z NaN throughout.  z: [T][latent] bf16; the activations enter
- * W3 rounded to fp16's 11 bits, everything else is fp32 up to z.  0 <= T <= 1024, 1 <= top_k
+ * W3 rounded to fp16's 11 bits, everything else is fp32 up to z.  (Batches of more than a few
+ * assignments are grouped by expert; they are summed as bf16 results of lmoe_w4_matvec
+ * are, with what is said there, and the others as its fp32 results.)  0 <= T <= 1024, 1 <= top_k
  * <= 32, n_experts <= 1024, latent, inter <= 32768; T = 0 enqueues nothing.
  * workspace: 256-byte aligned, not shared with a call that may run at the same
  * time. */

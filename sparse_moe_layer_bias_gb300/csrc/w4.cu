@@ -10,14 +10,17 @@
 // else is small: the kernels are bound by HBM, and next by the ALU that takes the
 // codes apart.  The inner sums run on mma.sync m16n8k16 (16 weight rows x 8
 // columns): u - 8 is exact in fp16, x is taken to fp16 by a power of two that
-// brings the largest of a token's values in the warp's columns to 2^14..2^15
-// (what that cuts off is below 2^-38 of it), the products are exact and are
+// brings the largest of a token's values in the warp's columns (in
+// w4_rows_kernel, of its row) to 2^14..2^15 (which cuts off at most 2^-35 of it: half of
+// the columns are held divided by 16, the others lose 2^-39), the products are exact and are
 // summed in fp32, and each group's sum is scaled in fp32 afterwards, so nothing
 // is rounded below fp32.  (fp16 rather than bf16 because its 10 bits of mantissa
 // take two codes out of one shifted word: 5 ALU operations for 8 codes instead of
 // 7.  tcgen05.mma would need the weights as 16-bit values in shared memory, four
 // times the bytes written back through it; a warp's own mma takes them from
-// registers.)
+// registers.)  The experts' activations are fp32 and enter W3 the same way, rounded to
+// fp16's 11 bits: 2^-12 of each, a sixteenth of what z's rounding to bf16 may take.
+// Two fp16 halves would keep them whole, for twice the mma.
 //
 // Two kernels share this: w4_kernel, whose warps split a row's columns, and further down
 // w4_rows_kernel, whose warps take whole rows; which one a call takes is said at
@@ -38,7 +41,7 @@
 // group's products only the columns that hold its part are added up.  The warps of
 // a block that share a row tile add their sums through shared memory.  For one token
 // the time is latency, not bandwidth: a token's 16 of 896 experts (3584 x 512, group 32) take
-// 27.2 us in two launches, 49.6 MB; 14336 x 1024 by one row 6.0 us, 8.3 MB.
+// 27.8 us in two launches, 49.6 MB; 14336 x 1024 by one row 6.0 us, 8.3 MB.
 // (Tasks half as wide, for twice the warps: no faster, 28.5 us against 28.5 then.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -643,8 +646,8 @@ __global__ void __launch_bounds__(THREADS) __maxnreg__(P == 8 ? 128 : 96) w4_ker
 // dependent reads and of conversion), the warps' unequal ends and rounds of units that do not fill
 // the blocks.  (Asking for a unit's first items ahead of that by prefetches into L2 made it slower, by
 // 1 to 6%: the copies wait behind them.)  Measured: 65536 x 7168 by 8 rows 48 us, 5.1 TB/s;
-// 64 tokens of top-16 over 896 experts (3584 x 512) 304 us in five launches, 4.5 TB/s; 6 such
-// tokens 81 us.
+// 64 tokens of top-16 over 896 experts (3584 x 512) 306 us in five launches, 4.5 TB/s (in some runs
+// 328); 6 such tokens 82 us.
 //
 // Where the result is rounded to bf16 anyway (FAST), the codes are not taken down to
 // u - 8: the products with 1024 + u and 16 (64 + u), as they come out of the masks, are
